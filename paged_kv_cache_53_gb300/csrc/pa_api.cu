@@ -962,13 +962,26 @@ int pa_prefill_mass(void* out, pa_dtype out_dtype, const void* q, const void* k_
                         max_blocks_per_seq, cu_q_lens, context_lens, num_seqs, num_tokens, max_q,
                         max_ctx, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
                         scale, dtype, workspace, workspace_bytes, stream, a, &empty);
-  if (rc != PA_OK || empty) return rc;
+  if (rc != PA_OK || num_seqs == 0) return rc;
   if (num_seqs > 65535 || num_kv_heads > 65535)
     return fail(PA_ERR_UNSUPPORTED, "%s: more than 65535 sequences or KV heads", who);
+  if (max_blocks_per_seq <= 0)
+    return fail(PA_ERR_INVALID_ARG, "%s: max_blocks_per_seq must be > 0", who);
   MassTarget m;
   rc = mass_args(who, mass, mass_stride, mass_rows, num_mass_rows, decay, num_seqs, max_ctx,
                  max_blocks_per_seq, block_size, m);
   if (rc != PA_OK) return rc;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (empty) {  // no query, but decay is applied once a call
+    if (!context_lens) return fail(PA_ERR_INVALID_ARG, "%s: null pointer", who);
+    if (decay == 1.f) return PA_OK;
+    int32_t* st = status_word(stream);
+    if (st == nullptr) return fail(PA_ERR_CUDA, "%s: no usable CUDA device", who);
+    const int cap = (int)std::min<long long>(max_ctx, (long long)max_blocks_per_seq * block_size);
+    const cudaError_t e = launch_mass_decay(m, context_lens, num_seqs, num_kv_heads, cap, st, s);
+    if (e != cudaSuccess) return fail(PA_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+    return PA_OK;
+  }
   const size_t need = pa_prefill_mass_workspace_bytes(num_seqs, num_tokens, max_q, num_q_heads,
                                                       num_kv_heads, head_dim, max_ctx, block_size);
   if (workspace_bytes < need)
@@ -981,7 +994,6 @@ int pa_prefill_mass(void* out, pa_dtype out_dtype, const void* q, const void* k_
   a.tile_starts = reinterpret_cast<int*>(ws);
   a.tile_keys = prefill_mass_item_keys(num_seqs, num_kv_heads, max_ctx);
   a.lse = reinterpret_cast<float*>(ws + align_up(sizeof(int) * ((size_t)num_seqs + 1), 256));
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
   rc = launch_prefill(a, s);
   return rc != PA_OK ? rc : launch_prefill_mass(a, observe, m, s);
 }

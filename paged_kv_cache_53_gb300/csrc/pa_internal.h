@@ -282,6 +282,11 @@ int launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 // Keys per item of launch_prefill_mass for these sizes.
 int prefill_mass_item_keys(int num_seqs, int num_kv_heads, int max_ctx);
 
+// mass = decay * mass over every context: what a call of no tokens leaves to do.
+cudaError_t launch_mass_decay(const MassTarget& mass, const int32_t* context_lens, int num_seqs,
+                              int num_kv_heads, int ctx_cap, int32_t* status,
+                              cudaStream_t stream);
+
 // The chunk's attention weights accumulated per cached position (pa_prefill_mass.cu), from
 // the lse of launch_prefill.  `observe`: queries at each chunk's end that count (null: all).
 int launch_prefill_mass(const PrefillArgs& a, const int32_t* observe, const MassTarget& mass,

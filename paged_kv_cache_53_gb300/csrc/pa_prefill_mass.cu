@@ -533,6 +533,31 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
+// A call without queries: decay alone, over every context.  The same product, rounded once, as the
+// weights of an item without query tiles end on.  Bound by HBM, at few positions by the launch.
+constexpr int kDecayThreads = 256, kDecayPerThread = 4;
+__global__ void __launch_bounds__(kDecayThreads)
+    mass_decay_kernel(const MassTarget mass, const int32_t* context_lens, int num_kv_heads,
+                      int ctx_cap, int32_t* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int ctx = __ldg(context_lens + b);
+  if (ctx == 0) return;
+  const int row = mass.rows != nullptr ? __ldg(mass.rows + b) : b;
+  if (ctx < 0 || ctx > ctx_cap || row < 0 || row >= mass.num_rows) {
+    if (threadIdx.x == 0) flag_status(status, PA_STATUS_BAD_CONTEXT);
+    return;
+  }
+  float* m = mass.mass + ((size_t)row * num_kv_heads + h) * mass.stride;
+  const long long first = (long long)blockIdx.x * kDecayThreads * kDecayPerThread + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < kDecayPerThread; ++i) {
+    const long long at = first + i * kDecayThreads;
+    if (at < ctx) m[at] = mass.decay != 0.f ? mass.decay * m[at] : 0.f;  // (0: not read)
+  }
+}
+
 constexpr int kMaxDev = 64;
 std::mutex g_mutex;
 
@@ -618,6 +643,17 @@ int launch_prefill_mass(const PrefillArgs& a, const int32_t* observe, const Mass
   const int ctx_cap = (int)std::min<long long>(a.max_ctx, (long long)a.max_blocks * a.block_size);
   return a.dtype == PA_BF16 ? dispatch<__nv_bfloat16>(a, p, ctx_cap, a.tile_keys, stream)
                             : dispatch<__half>(a, p, ctx_cap, a.tile_keys, stream);
+}
+
+cudaError_t launch_mass_decay(const MassTarget& mass, const int32_t* context_lens, int num_seqs,
+                              int num_kv_heads, int ctx_cap, int32_t* status,
+                              cudaStream_t stream) {
+  constexpr int kPositions = kDecayThreads * kDecayPerThread;
+  // (a context's status is looked at even where none may have a position)
+  const unsigned x = (unsigned)std::max(1, ctx_cap / kPositions + (ctx_cap % kPositions != 0));
+  return launch_pdl(mass_decay_kernel, dim3(x, (unsigned)num_kv_heads, (unsigned)num_seqs),
+                    dim3(kDecayThreads), 0, stream, mass, context_lens, num_kv_heads, ctx_cap,
+                    status);
 }
 
 int prefill_mass_item_keys(int num_seqs, int num_kv_heads, int max_ctx) {
