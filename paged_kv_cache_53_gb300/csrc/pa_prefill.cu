@@ -158,7 +158,12 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int b = tid; b < num_seqs; b += blockDim.x) {
     const int chunk = cu_q_lens[b + 1] - cu_q_lens[b];
     const int ctx0 = context_lens[b] - chunk;
-    if (chunk <= 0) continue;
+    if (chunk <= 0) {
+      // an empty chunk has a length to check where the weights of its context fade
+      if (tile_starts != nullptr && (context_lens[b] < 0 || context_lens[b] > max_ctx))
+        flag_status(status, PA_STATUS_BAD_CONTEXT);
+      continue;
+    }
     if (ctx0 < 0 || context_lens[b] > max_ctx) {  // such a sequence gets no output rows
       flag_status(status, PA_STATUS_BAD_CONTEXT);
       continue;

@@ -120,6 +120,16 @@ def test_bad_rows_and_contexts_without_tokens(pa):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ctx", [-3, 101])
+def test_bad_contexts_of_empty_chunks_beside_a_query(pa, ctx):
+    pa.get_status()
+    old = torch.rand(3, HKV, 112, device="cuda")
+    got = _run(pa, [ctx, 30], [0, 7], old.clone(), None, 0.5, 100)
+    assert pa.get_status() == pa.STATUS_BAD_CONTEXT
+    assert torch.equal(got[[0, 2]], old[[0, 2]]) and not torch.equal(got[1], old[1])
+
+
+@pytest.mark.gpu
 def test_captured_and_replayed(pa):
     pa.get_status()
     old = torch.rand(2, HKV, 100, device="cuda")
