@@ -539,7 +539,8 @@ int pa_decode_mass(void* out, pa_dtype out_dtype, const void* q, const void* k_c
  * once a call, to a sequence whose chunk is empty too; with num_tokens = 0, where every chunk is,
  * the call does that alone (with decay 1 nothing) and needs neither q and out nor a workspace.  A
  * sequence whose context is negative or longer than max_ctx or its table sets
- * PA_STATUS_BAD_CONTEXT and its mass is left alone.  Every other argument as in pa_prefill_chunk.  Equal calls give equal bits.
+ * PA_STATUS_BAD_CONTEXT and its mass is left alone.  Every other argument as in pa_prefill_chunk.
+ * Equal calls give equal bits.
  */
 size_t pa_prefill_mass_workspace_bytes(int num_seqs, int num_tokens, int max_q, int num_q_heads,
                                        int num_kv_heads, int head_dim, int max_ctx,

@@ -410,26 +410,29 @@ def rotary_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_n
     """Rotary positions of a step's queries and keys, and the cache write of the turned keys and
     the values (see pa_rotary_append).  q, k_new, v_new [T, H, D] may be views with a token
     stride; positions int32 [axes, T]; cu_q_lens None: one new token per sequence."""
-    nb, h_kv, bs, d = k_cache.shape
+    cache, rows = k_cache.shape, q.shape
+    nb, h_kv, bs, d = cache
     dtype = k_cache.dtype
-    if q.dim() != 3:
+    if len(rows) != 3:
         raise ValueError("q must be [tokens, heads, dim]")
-    t, h_q, _ = q.shape
+    t, h_q, _ = rows
     qp, qs = _token_rows(q, dtype, (t, h_q, d), "q")
     kp, ks = _token_rows(k_new, dtype, (t, h_kv, d), "k_new")
     vp, vs = _token_rows(v_new, dtype, (t, h_kv, d), "v_new")
     if q_out.dtype != dtype or v_cache.dtype != dtype:
         raise TypeError(f"q_out and the caches must be {dtype}")
-    if q_out.shape != q.shape or v_cache.shape != k_cache.shape:
+    if q_out.shape != rows or v_cache.shape != cache:
         raise ValueError("q_out must be like q, and the caches alike")
     i32 = torch.int32
     if (block_tables.dtype != i32 or context_lens.dtype != i32 or positions.dtype != i32 or
             (cu_q_lens is not None and cu_q_lens.dtype != i32)):
         raise TypeError("block_tables, cu_q_lens, context_lens and positions must be int32")
     b = context_lens.shape[0]
-    if positions.dim() != 2 or positions.shape[1] != t:
+    axes = positions.shape
+    if len(axes) != 2 or axes[1] != t:
         raise ValueError("positions must be [axes, tokens]")
-    if block_tables.shape[0] != b:
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != b:
         raise ValueError("block_tables must have a row per sequence")
     if cu_q_lens is not None:
         if cu_q_lens.shape[0] != b + 1:
@@ -440,45 +443,53 @@ def rotary_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_n
         raise TypeError("slots must be int64 [tokens]")
     _check(lib().pa_rotary_append(
         _ptr(q_out), qp, qs, kp, ks, vp, vs, _ptr(k_cache), _ptr(v_cache), _ptr(slots),
-        _ptr(block_tables), block_tables.shape[1], _ptr(cu_q_lens), _ptr(context_lens),
-        _ptr(positions), positions.shape[0], rotary.inv_freq, rotary.pair_axis,
+        _ptr(block_tables), tables[1], _ptr(cu_q_lens), _ptr(context_lens),
+        _ptr(positions), axes[0], rotary.inv_freq, rotary.pair_axis,
         rotary.rotary_dim, rotary.interleaved, b, t, h_q, h_kv, d, bs, nb, _DT[dtype],
-        _stream_for(k_cache, stream)))
+        _stream_for(stream, q_out, q, k_new, v_new, k_cache, v_cache, block_tables, cu_q_lens,
+                    context_lens, positions, slots)))
 
 
-def _stream_for(t: torch.Tensor, stream) -> int:
-    """The stream's handle; the caches `t` have to be on the current device."""
+def _stream_for(stream, *tensors: Optional[torch.Tensor]) -> int:
+    """The stream's handle; every tensor of the call has to be on the current device, since
+    the kernels take its address as it is."""
     device = torch.cuda.current_device()
-    if t.get_device() != device:
-        raise ValueError("the tensors must be on the current device")
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"the tensors must be on the current device (cuda:{device}): one of "
+                             f"{t.dtype} {list(t.shape)} is on {t.device}")
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 def _attention_args(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
                     v_cache: torch.Tensor, block_tables: torch.Tensor,
                     context_lens: torch.Tensor):
-    """Shapes and types that the C call cannot see."""
-    if q.dim() != 3 or out.shape != q.shape or q.shape[2] != k_cache.shape[3]:
+    """Shapes and types that the C call cannot see.  Returns the shapes of q, the caches and the
+    block tables, and the number of sequences."""
+    rows, cache, tables, b = q.shape, k_cache.shape, block_tables.shape, context_lens.shape[0]
+    if len(rows) != 3 or out.shape != rows or rows[2] != cache[3]:
         raise ValueError("q and out must be [tokens, heads, dim] alike, dim that of the caches")
-    if v_cache.shape != k_cache.shape:
+    if v_cache.shape != cache:
         raise ValueError("the two caches must be alike")
-    if q.dtype != k_cache.dtype or v_cache.dtype != k_cache.dtype:
+    if not q.dtype == v_cache.dtype == k_cache.dtype:
         raise TypeError("q and the caches must have one type")
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    if not block_tables.dtype == context_lens.dtype == torch.int32:
         raise TypeError("block_tables and context_lens must be int32")
-    if block_tables.shape[0] != context_lens.shape[0]:
+    if len(tables) != 2 or tables[0] != b:
         raise ValueError("block_tables must have a row per sequence")
+    return rows, cache, tables, b
 
 
 def _mass(mass: torch.Tensor, mass_rows: Optional[torch.Tensor], h_kv: int, b: int):
     """(pointer, stride, rows pointer, rows) of a [rows, H_kv, positions] mass."""
-    if mass.dtype != torch.float32 or mass.dim() != 3 or mass.shape[1] != h_kv:
+    shape = mass.shape
+    if mass.dtype != torch.float32 or len(shape) != 3 or shape[1] != h_kv:
         raise TypeError("mass must be float32 [rows, H_kv, positions]")
     if mass_rows is not None:
         _i32(mass_rows, "mass_rows")
         if mass_rows.numel() != b:
             raise ValueError("mass_rows must have one entry per sequence")
-    return _ptr(mass), mass.shape[2], _ptr(mass_rows), mass.shape[0]
+    return _ptr(mass), shape[2], _ptr(mass_rows), shape[0]
 
 
 def decode_mass_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -493,18 +504,18 @@ def decode_mass(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cac
                 mass_rows: Optional[torch.Tensor] = None, decay: float = 1.0, stream=None):
     """Paged decode attention that also adds every position's attention weight to `mass`
     (float32 [rows, H_kv, positions], see pa_decode_mass)."""
-    nb, h_kv, bs, d = k_cache.shape
-    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens)
-    b, h_q, _ = q.shape
-    if context_lens.shape[0] != b:
+    (t, h_q, _), (nb, h_kv, bs, d), tables, b = _attention_args(out, q, k_cache, v_cache,
+                                                                 block_tables, context_lens)
+    if t != b:
         raise ValueError("q must have a row per sequence")
     m, ms, mr, nr = _mass(mass, mass_rows, h_kv, b)
     _check(lib().pa_decode_mass(_ptr(out), dtype_code(out.dtype), _ptr(q), _ptr(k_cache),
-                                _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+                                _ptr(v_cache), _ptr(block_tables), tables[1],
                                 _ptr(context_lens), max_ctx, m, ms, mr, nr, float(decay), b, h_q,
                                 h_kv, d, bs, nb, float(scale), dtype_code(k_cache.dtype),
                                 _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                _stream_for(k_cache, stream)))
+                                _stream_for(stream, out, q, k_cache, v_cache, block_tables,
+                                            context_lens, mass, mass_rows, workspace)))
 
 
 def prefill_mass_workspace_bytes(num_seqs: int, num_tokens: int, max_q: int, num_q_heads: int,
@@ -522,10 +533,8 @@ def prefill_mass(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_ca
     """Causal chunked-prefill attention that also adds the weights its queries (or, with
     `observe`, the last observe[b] of each chunk) give every position to `mass` (see
     pa_prefill_mass)."""
-    nb, h_kv, bs, d = k_cache.shape
-    _attention_args(out, q, k_cache, v_cache, block_tables, context_lens)
-    t, h_q, _ = q.shape
-    b = context_lens.shape[0]
+    (t, h_q, _), (nb, h_kv, bs, d), tables, b = _attention_args(out, q, k_cache, v_cache,
+                                                                 block_tables, context_lens)
     _i32(cu_q_lens, "cu_q_lens")
     if cu_q_lens.shape[0] != b + 1:
         raise ValueError("cu_q_lens must have one entry more than context_lens")
@@ -535,12 +544,14 @@ def prefill_mass(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_ca
         if observe.numel() != b:
             raise ValueError("observe must have one entry per sequence")
     _check(lib().pa_prefill_mass(_ptr(out), dtype_code(out.dtype), _ptr(q), _ptr(k_cache),
-                                 _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+                                 _ptr(v_cache), _ptr(block_tables), tables[1],
                                  _ptr(cu_q_lens), _ptr(context_lens), _ptr(observe), max_q,
                                  max_ctx, m, ms, mr, nr, float(decay), b, t, h_q, h_kv, d, bs, nb,
                                  float(scale), dtype_code(k_cache.dtype), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(),
-                                 _stream_for(k_cache, stream)))
+                                 _stream_for(stream, out, q, k_cache, v_cache, block_tables,
+                                             cu_q_lens, context_lens, observe, mass, mass_rows,
+                                             workspace)))
 
 
 def evict_workspace_bytes(num_seqs: int, num_kv_heads: int, max_ctx: int, max_keep: int) -> int:
@@ -555,29 +566,32 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, mass: torch.Tensor,
     """Cuts every sequence's cache down to its keep_lens[b] weightiest positions per KV head,
     in place or into new blocks (see pa_evict).  `kept` int32 [sequences, H_kv, max_keep]
     receives the kept positions, new_context_lens the new lengths."""
-    nb, h_kv, bs, d = k_cache.shape
-    b = context_lens.shape[0]
+    cache, tables, new_tables = k_cache.shape, block_tables.shape, new_block_tables.shape
+    nb, h_kv, bs, d = cache
+    b, lists = context_lens.shape[0], kept.shape
     i32 = torch.int32
     if not (block_tables.dtype == new_block_tables.dtype == context_lens.dtype ==
             keep_lens.dtype == new_context_lens.dtype == kept.dtype == i32):
         raise TypeError("tables, lengths and kept must be int32")
-    if (block_tables.shape[0] != b or new_block_tables.shape[0] != b or
-            keep_lens.shape[0] != b or new_context_lens.shape[0] != b):
+    if (len(tables) != 2 or len(new_tables) != 2 or
+            not tables[0] == new_tables[0] == keep_lens.shape[0] == new_context_lens.shape[0] == b):
         raise ValueError("tables and lengths must have an entry per sequence")
-    if kept.dim() != 3 or kept.shape[0] != b or kept.shape[1] != h_kv:
+    if len(lists) != 3 or lists[0] != b or lists[1] != h_kv:
         raise ValueError("kept must be [sequences, H_kv, max_keep]")
     if new_mass.shape != mass.shape or new_mass.dtype != mass.dtype:
         raise ValueError("new_mass must be like mass")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    if v_cache.shape != cache or v_cache.dtype != k_cache.dtype:
         raise ValueError("the two caches must be alike")
     m, ms, mr, nr = _mass(mass, mass_rows, h_kv, b)
     _check(lib().pa_evict(_ptr(k_cache), _ptr(v_cache), m, _ptr(new_mass), ms, mr, nr,
-                          _ptr(block_tables), block_tables.shape[1], _ptr(new_block_tables),
-                          new_block_tables.shape[1], _ptr(context_lens), _ptr(keep_lens), max_ctx,
-                          kept.shape[2], int(sinks), int(recent), _ptr(new_context_lens),
+                          _ptr(block_tables), tables[1], _ptr(new_block_tables),
+                          new_tables[1], _ptr(context_lens), _ptr(keep_lens), max_ctx,
+                          lists[2], int(sinks), int(recent), _ptr(new_context_lens),
                           _ptr(kept), b, h_kv, d, bs, nb, dtype_code(k_cache.dtype),
                           _ptr(workspace), workspace.numel() * workspace.element_size(),
-                          _stream_for(k_cache, stream)))
+                          _stream_for(stream, k_cache, v_cache, mass, new_mass, block_tables,
+                                      new_block_tables, context_lens, keep_lens,
+                                      new_context_lens, kept, mass_rows, workspace)))
 
 
 def testing_decode_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int,
