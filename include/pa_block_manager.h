@@ -109,7 +109,9 @@ int pa_bm_fork(pa_block_manager* bm, int64_t parent_id, int64_t child_id);
 /* Cuts n distinct resident sequences down to num_tokens[i] tokens each (1 .. its tokens), for
  * pa_evict: take the tables before this call (pa_bm_block_tables: pa_evict's block_tables) and
  * after it (its new_block_tables), with num_tokens as keep_lens.  Sequences that one pa_evict
- * call cuts go into one call of this.  Copy-on-write pairs queued earlier must be copied first.
+ * call cuts go into one call of this.  Copy-on-write pairs queued earlier must be taken
+ * (pa_bm_take_copies) and copied first: a call that cuts anything while some are queued is refused
+ * with PA_ERR_INVALID_ARG.
  * The blocks it frees may be reused by work that follows the pa_evict on its stream.
  * All or nothing; num_tokens[i] equal to the sequence's tokens leaves it as it is. */
 int pa_bm_evict(pa_block_manager* bm, const int64_t* seq_ids, int n, const int32_t* num_tokens);

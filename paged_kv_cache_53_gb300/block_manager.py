@@ -146,7 +146,8 @@ class BlockManager:
 
     def evict(self, seq_ids: Sequence[int], num_tokens: Sequence[int]):
         """Cuts sequence seq_ids[i] down to num_tokens[i] tokens for `evict` on the device: its
-        block_tables are the tables before this call, its new_block_tables those after."""
+        block_tables are the tables before this call, its new_block_tables those after.  Queued
+        copy-on-write pairs have to be taken and copied first."""
         s, sp = _arr(seq_ids, np.int64)
         t, tp = _arr(num_tokens, np.int32)
         if t.size != s.size:

@@ -350,6 +350,7 @@ int pa_bm_evict(pa_block_manager* bm, const int64_t* seq_ids, int n, const int32
   std::vector<std::vector<bool>> replaced;
   std::vector<std::vector<int32_t>> old;  // the tables before
   int64_t need = 0;
+  bool cuts = false;
   try {
     seqs.reserve(n);
     replaced.reserve(n);
@@ -367,6 +368,7 @@ int pa_bm_evict(pa_block_manager* bm, const int64_t* seq_ids, int n, const int32
       seqs.push_back(s);
       std::vector<bool> r;
       if (num_tokens[i] < s->tokens) {
+        cuts = true;
         r.resize((size_t)cdiv(num_tokens[i], bm->bs));
         for (size_t j = 0; j < r.size(); ++j) {
           r[j] = bm->ref[s->blocks[j]] > 1;
@@ -379,6 +381,10 @@ int pa_bm_evict(pa_block_manager* bm, const int64_t* seq_ids, int n, const int32
   } catch (...) {
     return pa::fail(PA_ERR_INVALID_ARG, "pa_bm_evict: out of host memory");
   }
+  // a queued copy's source or target may be a block that is rewritten or freed here
+  if (cuts && !bm->copies.empty())
+    return pa::fail(PA_ERR_INVALID_ARG, "pa_bm_evict: %d copy-on-write pairs are queued",
+                    (int)(bm->copies.size() / 2));
   if (need > bm->queued)
     return pa::fail(PA_ERR_NO_BLOCKS, "pa_bm_evict: %lld blocks needed, %d free", (long long)need,
                     bm->queued);
