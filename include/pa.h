@@ -475,10 +475,10 @@ int pa_mixed_step(const pa_decode_batch* dec, const pa_prefill_batch* pre, void*
  *               from cu_q_lens[num_seqs] on (padding) are left alone: no row of theirs is
  *               written
  *   positions   int32 [num_axes, num_tokens], device; any sign and size
- *   inv_freq    HOST double [rotary_dim / 2], radians per position, finite
+ *   inv_freq    HOST double [rotary_dim / 2], radians per position, each at most 2^32 either way
  *   pair_axis   HOST int32 [rotary_dim / 2], each in [0, num_axes); num_axes <= 4
  *   rotary_dim  even, 2 .. head_dim
- * The host arrays are read during the call only.  Angles are exact to 2^-26 turns at any
+ * The host arrays are read during the call only.  Angles are exact to 2^-26 + 2^-31 turns at any
  * position; the products are fp32, rounded once to dtype.  A token without a valid slot
  * sets a status bit as in pa_cache_append; its query is still turned.  V is a bit copy.
  */

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1024,6 +1025,9 @@ int pa_rotary_append(void* q_out, const void* q, int64_t q_stride, const void* k
   for (int i = 0; i < rotary_dim / 2; ++i) {
     if (!(inv_freq[i] - inv_freq[i] == 0.0))
       return fail(PA_ERR_INVALID_ARG, "%s: inv_freq[%d] is not finite", who, i);
+    if (!(std::fabs(inv_freq[i]) <= kMaxRotaryFreq))
+      return fail(PA_ERR_INVALID_ARG, "%s: inv_freq[%d] = %g is beyond 2^32 radians a position", who,
+                  i, inv_freq[i]);
     if (pair_axis[i] < 0 || pair_axis[i] >= num_axes)
       return fail(PA_ERR_INVALID_ARG, "%s: pair_axis[%d] = %d outside [0, %d)", who, i,
                   pair_axis[i], num_axes);

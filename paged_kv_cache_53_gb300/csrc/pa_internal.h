@@ -77,6 +77,7 @@ cudaError_t launch_copy_blocks(void* const* k_caches, void* const* v_caches, int
 // ----------------------------------------------------------------------------------
 constexpr int kMaxRotaryPairs = 64;  // half of the largest head_dim
 constexpr int kMaxRotaryAxes = 4;
+constexpr double kMaxRotaryFreq = 0x1p32;  // radians a position, of either sign
 
 struct RotaryArgs {
   void* q_out;

@@ -253,8 +253,9 @@ __global__ void __launch_bounds__(kThreads) rotary_append_kernel(
 }
 
 // A frequency in radians as turns in 64-bit fixed point, whole turns dropped.  1 / 2 pi is
-// carried as the sum of two doubles, so that the result is good to its last bits and a
-// position of 2^31 still has its angle to 2^-33 turns.
+// carried as the sum of two doubles, good to 2^-107 of itself: up to kMaxRotaryFreq that is far
+// below the two truncations (2^-64 turns each), so that a position of 2^31 still has its angle to
+// 2^-32 turns.
 unsigned long long turns_per_position(double freq) {
   const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
   const double q = freq * hi;
