@@ -394,13 +394,12 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm)
         v[kHalf + u] = p.v_cache[at];
       }
     }
-#pragma unroll
-    for (int u = 0; u < kMoveVecs; ++u)  // (arrived, not only asked for, before it is said)
-      asm volatile("" ::"r"(v[u].x), "r"(v[u].y), "r"(v[u].z), "r"(v[u].w) : "memory");
-    __syncthreads();  // the tile is read
+    __syncthreads();
     if (warp == 0) {
       uint32_t* done = p.done + (size_t)bh * p.done_words;
       if (lane == 0) {
+        // the barrier orders every thread's loads before this fence, and the fence before the bit:
+        // no store that follows the bit's reading can reach them
         __threadfence();
         atomicOr(done + (tile >> 5), 1u << (tile & 31));
       }
