@@ -1706,14 +1706,6 @@ __global__ void __launch_bounds__(128) decode_f32_kernel(const float* __restrict
 // 4. accumulated weights
 // ----------------------------------------------------------------------------------
 
-struct MassParams {
-  float* mass;  // [rows, H_kv, stride]
-  long long stride;
-  const int32_t* rows;  // null: sequence b has row b
-  int num_rows;
-  float decay;
-};
-
 // mass[row][h][j] = decay * mass[row][h][j] + sum over h's query heads of P_j, one warp per chunk
 // of positions of a (partition, KV head) unit of the plan at a time.  P_j = 2^(score - lse) from
 // the scores the attention kernel left, with lse = M + log2 L over the sequence's partials, which
@@ -1722,7 +1714,7 @@ struct MassParams {
 // Chunks hold 128 positions or, in batches with more than two of those for each warp, or where the
 // partials that an lse is made of would be the larger part of a chunk's reads, up to 1,024.
 template <int G>
-__device__ __forceinline__ void add_mass(const DecodeParams& p, const MassParams& mp, int first,
+__device__ __forceinline__ void add_mass(const DecodeParams& p, const MassTarget& mp, int first,
                                          int stride, int lane) {
   constexpr int PP = G <= 4 ? 4 : G == 8 ? 2 : 1;  // positions a lane has in flight
   const int units = __ldcg(p.ws.header + 1), psz = __ldcg(p.ws.header + 2);
@@ -1816,7 +1808,7 @@ __device__ __forceinline__ void add_mass(const DecodeParams& p, const MassParams
 // no weights to add start on the rows (which are dealt out from the other end).
 template <int D, typename TO, bool CTA, int G>
 __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtasPerSm)
-    decode_finish_kernel(const DecodeParams p, const MassParams mp) {
+    decode_finish_kernel(const DecodeParams p, const MassTarget mp) {
   const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   const int warps = gridDim.x * kMergeWarps;
   Merge<D, TO, CTA> merge(p, CTA ? gridDim.x - 1 - blockIdx.x : warps - 1 - warp,
@@ -1825,7 +1817,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kMergeCtasPerSm)
   merge.run(lane);
 }
 
-using FinishKernel = void (*)(DecodeParams, MassParams);
+using FinishKernel = void (*)(DecodeParams, MassTarget);
 template <int D, typename TO, bool CTA>
 FinishKernel finish_kernel_for_group(int group) {
   switch (group) {
@@ -2099,7 +2091,6 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
   const long long rows = (long long)a.num_seqs * a.num_q_heads;
   const int wave = sm_count() * kMergeCtasPerSm;
   if (mass) {
-    const MassParams mp = {a.mass.mass, a.mass.stride, a.mass.rows, a.mass.num_rows, a.mass.decay};
     const bool by_cta = merge_by_cta(rows, sm_count());
     const FinishKernel finish =
         a.head_dim == 128 ? (by_cta ? finish_kernel_for<128, true>(a.out_dtype, p.group)
@@ -2114,7 +2105,7 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     const long long ctas = (units + kMergeWarps - 1) / kMergeWarps +
                            (by_cta ? rows : (rows + kMergeWarps - 1) / kMergeWarps);
     e = launch_pdl(finish, dim3((unsigned)std::max(1ll, std::min<long long>(ctas, wave))),
-                   dim3(256), 0, stream, p, mp);
+                   dim3(256), 0, stream, p, a.mass);
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "pa_decode (mass): %s", cudaGetErrorString(e));
     return PA_OK;
   }
