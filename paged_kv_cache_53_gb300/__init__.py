@@ -445,7 +445,7 @@ def rotary_append(q_out: torch.Tensor, q: torch.Tensor, k_new: torch.Tensor, v_n
         _ptr(q_out), qp, qs, kp, ks, vp, vs, _ptr(k_cache), _ptr(v_cache), _ptr(slots),
         _ptr(block_tables), tables[1], _ptr(cu_q_lens), _ptr(context_lens),
         _ptr(positions), axes[0], rotary.inv_freq, rotary.pair_axis,
-        rotary.rotary_dim, rotary.interleaved, b, t, h_q, h_kv, d, bs, nb, _DT[dtype],
+        rotary.rotary_dim, rotary.interleaved, b, t, h_q, h_kv, d, bs, nb, dtype_code(dtype),
         _stream_for(stream, q_out, q, k_new, v_new, k_cache, v_cache, block_tables, cu_q_lens,
                     context_lens, positions, slots)))
 

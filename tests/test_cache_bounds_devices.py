@@ -60,3 +60,19 @@ def test_every_tensor_has_to_be_on_the_current_device(name, monkeypatch):
             with pytest.raises(ValueError, match="current device"):
                 call(**{**here, k: elsewhere}, **others)
             assert len(reached) == 1, k
+
+
+@pytest.mark.parametrize("name", ["rotary_append", "decode_mass", "prefill_mass", "evict"])
+def test_a_type_that_is_not_built_is_a_type_error(name, monkeypatch):
+    import paged_kv_cache_53_gb300 as pa
+    reached = []
+    monkeypatch.setattr(pa, "_lib", SimpleNamespace(**{
+        "pa_" + name: lambda *a: reached.append(a) or 0}))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    tensors, others = _calls(pa)[name]
+    others["stream"] = SimpleNamespace(cuda_stream=0)
+    wide = {k: (t.double() if k in ("out", "q", "q_out", "k_new", "v_new", "k_cache", "v_cache")
+                else t).as_subclass(OnDevice) for k, t in tensors.items()}
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        getattr(pa, name)(**wide, **others)
+    assert not reached
