@@ -512,7 +512,8 @@ int pa_rotary_append(void* q_out, const void* q, int64_t q_stride, const void* k
  *   workspace  at least pa_decode_mass_workspace_bytes(...) bytes: pa_decode's and one fp32 per
  *              (sequence, query head, position of max_ctx)
  * Every other argument as in pa_decode.  The weights are fp32 (2^x within 2 ulp of a score
- * summed in fp32) and added in a fixed order: equal calls give equal bits.
+ * summed in fp32) and added in a fixed order: equal calls give equal bits.  In P V, P is a pair of
+ * 16-bit hi + lo terms of the cache's type, as in pa_decode (fp32 caches: fp32).
  */
 size_t pa_decode_mass_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
                                       int head_dim, int max_ctx, int block_size);
@@ -540,7 +541,9 @@ int pa_decode_mass(void* out, pa_dtype out_dtype, const void* q, const void* k_c
  * the call does that alone (with decay 1 nothing) and needs neither q and out nor a workspace.  A
  * sequence whose context is negative or longer than max_ctx or its table sets
  * PA_STATUS_BAD_CONTEXT and its mass is left alone.  Every other argument as in pa_prefill_chunk.
- * Equal calls give equal bits.
+ * Equal calls give equal bits.  The outputs are pa_prefill_chunk's, bit for bit, with its
+ * arithmetic in P V (P and V in fp16, or as its exact pass has them); the weights are made of fp32
+ * scores and 2^x, with no rounding to fewer bits.
  */
 size_t pa_prefill_mass_workspace_bytes(int num_seqs, int num_tokens, int max_q, int num_q_heads,
                                        int num_kv_heads, int head_dim, int max_ctx,

@@ -27,7 +27,9 @@
 // turns them into weights beside the merge (section 4 below): 256 contexts of up to 8,192 tokens,
 // 32 / 8 heads, bf16, 200 us, 0.90 of a copy's rate; 6 of up to 131,072, 4 KV heads, 174 us, 0.78.
 // fp32 caches take a CUDA-core variant of step 2 (tensor cores have no fp32 input path
-// that meets an fp32 tolerance).
+// that meets an fp32 tolerance): one token at a time per warp, bound by its own arithmetic and
+// latency (with weights, 256 contexts of up to 8,192 tokens, 32 / 8 heads: 2.28 ms, where their
+// bytes take 0.36).
 //
 // The decode is bound by HBM: every context token's K and V row is read once and each
 // byte feeds ~1 (MHA) to ~8 (group of 8) flops, far below the ridge point.  The design
@@ -380,8 +382,8 @@ __global__ void __launch_bounds__(1024, 1) decode_plan_kernel(const int32_t* __r
       r.pad0 = r.pad1 = 0;
       ws.parts[p + 1 < np ? fbase + p : tslot] = r;
     };
-    // a lane per sequence; the whole warp for each where one has many partitions (one context of
-    // 128k tokens, 512 of them: 26 us for the plan by one lane)
+    // a lane per sequence; the whole warp for each where one has many partitions (decode with
+    // weights of one context of 131,072 tokens, 4 KV heads, 512 of them: 76 us, by one lane 85)
     if (__any_sync(~0u, np > 32)) {
       for (int l = 0; l < 32; ++l) {
         const int lnp = __shfl_sync(~0u, np, l);
@@ -582,8 +584,7 @@ __global__ void __launch_bounds__(256, kMergeCtasPerSm) decode_merge_kernel(cons
 // The decode that accumulates weights merges a row by a whole CTA where the batch has few rows:
 // each warp takes an eighth of the partials, rescaling as it goes, and
 // the eight results join in shared memory.  A warp per row would leave most SMs empty while each
-// waits for one partial after the other (32 query heads of 6 contexts of up to 128k tokens: 66 us
-// for the merge alone).  The sums are in another order than a warp's, so pa_decode keeps the latter,
+// waits for one partial after the other.  The sums are in another order than a warp's, so pa_decode keeps the latter,
 // and its bits.
 constexpr int kMergeWarps = 8;
 template <int D>
@@ -687,8 +688,9 @@ struct Merge {
   }
 };
 
-// up to two rows per CTA (768 rows: 138 us a call where a warp per row takes 141; no difference at
-// 1,152; 32 rows of one context of 128k tokens: 90 us where a warp per 32 columns took 136)
+// up to two rows per CTA (32 rows of one context of 131,072 tokens, 4 KV heads: 76 us a call where a
+// warp per row takes 180; of one of 4,000, 8 KV heads, 19 and 46; 192 rows of six of up to 131,072,
+// 169 and 192; no difference at 768 rows)
 bool merge_by_cta(long long rows, int sms) { return rows <= 2ll * sms * kMergeCtasPerSm; }
 
 using MergeKernel = void (*)(DecodeParams);
@@ -1766,7 +1768,8 @@ __device__ __forceinline__ void add_mass(const DecodeParams& p, const MassTarget
       const float2* ml =
           p.ws.part_ml + (size_t)r.part_start * p.num_q_heads + h * G + lane % G;
       float M = kNegInf, L = 0.f;
-      constexpr int U = 8;  // loads in flight (a context of 128k tokens has 152 partials)
+      constexpr int U = 8;  // loads in flight (of six contexts of up to 131,072 tokens, 4 KV heads,
+                            // the longest has 152 partials; alone it has 512)
 #pragma unroll 1
       for (int q0 = lane / G; q0 < r.nparts; q0 += U * (32 / G)) {
         float2 v[U];
@@ -2098,8 +2101,8 @@ int launch_decode(const DecodeArgs& a, cudaStream_t stream) {
                           : (by_cta ? finish_kernel_for<64, true>(a.out_dtype, p.group)
                                     : finish_kernel_for<64, false>(a.out_dtype, p.group));
     // a warp for every unit that there may be, and CTAs of their own for the rows, in a grid of up to
-    // a wave (3 contexts of up to 200 tokens: 11.3 us a call where a whole wave took 13.2; one of
-    // 4,000, 24.8 and 26.3)
+    // a wave (replayed in a graph, 3 contexts of up to 200 tokens: 11.4 us where a whole wave takes
+    // 13.1; one of 4,000, 19.1 and 19.7)
     const long long units = (long long)a.num_seqs * a.num_kv_heads *
                             (p.ctx_cap / (kMinPartBlocks * a.block_size) + 1);
     const long long ctas = (units + kMergeWarps - 1) / kMergeWarps +

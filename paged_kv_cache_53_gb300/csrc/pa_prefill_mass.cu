@@ -27,7 +27,7 @@
 //              product and two 2^x per pair of columns, added up
 // Bound: one 2^x per (key, query row), 32 a clock and SM, which for a 128 x 128 tile are the 512
 // clocks its product takes the tensor core; the two overlap (8 chunks of 512 over contexts of up to
-// 16,896 tokens, 32 heads: 104 us where either alone would take 60; the rest is the hand-over of
+// 16,896 tokens, 32 heads: 108 us where either alone would take 60; the rest is the hand-over of
 // the S buffers between two SMs).  Queries before the first that sees
 // the item's first key, and those not observed, are never loaded, and no product is taken of
 // tiles wholly above the diagonal.
@@ -534,7 +534,8 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // A call without queries: decay alone, over every context.  The same product, rounded once, as the
-// weights of an item without query tiles end on.  Bound by HBM, at few positions by the launch.
+// weights of an item without query tiles end on.  Bound by HBM, at few positions by the launch (64
+// contexts of 8,192, 8 heads: 5.6 us of mostly L2 traffic, 0.90 of a copy's rate; 3 of 200: 1.6).
 constexpr int kDecayThreads = 256, kDecayPerThread = 4;
 __global__ void __launch_bounds__(kDecayThreads)
     mass_decay_kernel(const MassTarget mass, const int32_t* context_lens, int num_kv_heads,
