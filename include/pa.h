@@ -373,8 +373,10 @@ size_t pa_prefill_workspace_bytes(int num_seqs, int num_tokens, int max_q, int n
  *
  *   out           [num_tokens, num_q_heads, head_dim] of out_dtype (dtype or PA_F32)
  *   q             [num_tokens, num_q_heads, head_dim] of dtype (PA_F16 or PA_BF16)
- *   cu_q_lens     int32 [num_seqs + 1]; max_q >= every chunk length
- *   context_lens  int32 [num_seqs]; chunk_len <= context_lens[b] <= max_ctx
+ *   cu_q_lens     int32 [num_seqs + 1], within 0 .. num_tokens; max_q >= every chunk length
+ *   context_lens  int32 [num_seqs]; chunk_len <= context_lens[b] <= max_ctx.  A sequence whose
+ *                 lengths break these, as far as the call would leave its arrays, gets no output
+ *                 rows and sets PA_STATUS_BAD_CONTEXT
  *   workspace     device scratch of pa_prefill_workspace_bytes(...) bytes (may be 0)
  * QK^T and PV run on the tensor cores with fp32 accumulation.  P and V enter the PV
  * product in fp16 (unit roundoff 2^-11; bf16's 2^-8 alone would not meet a 2e-3 bound):

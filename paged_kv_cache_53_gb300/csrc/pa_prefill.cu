@@ -137,11 +137,11 @@ constexpr int kPlanThreads = 1024;
 // causal rows first and the grid ends on the short ones.
 __global__ void __launch_bounds__(kPlanThreads)
     prefill_plan_kernel(const int32_t* __restrict__ cu_q_lens,
-                        const int32_t* __restrict__ context_lens, int num_seqs,
-                        int num_kv_heads, int group, int rows_per_item, int bn, int key_shift,
-                        long long max_ctx, PrefillItem* __restrict__ items,
-                        int* __restrict__ header, int32_t* status,
-                        int* __restrict__ tile_starts, int tile_keys) {
+                        const int32_t* __restrict__ context_lens, int num_seqs, int num_tokens,
+                        int num_kv_heads, int group, int rows_per_item, int max_chunk,
+                        int bn, int key_shift, long long max_ctx,
+                        PrefillItem* __restrict__ items, int* __restrict__ header,
+                        int32_t* status, int* __restrict__ tile_starts, int tile_keys) {
   griddep_wait();
   griddep_launch_dependents();
   __shared__ int s_hist[kPlanBuckets];
@@ -150,20 +150,28 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int i = tid; i < kPlanBuckets; i += blockDim.x) s_hist[i] = 0;
   __syncthreads();
   const int tpt = rows_per_item / group;  // chunk tokens per item
+  // sequence b's chunk length; kNoRoom for a chunk that the list, as long as max_q makes it, or
+  // the rows of q have no room for (and below 0 where the starts decrease: no chunk)
+  constexpr int kNoRoom = -0x7fffffff;
+  auto chunk_of = [&](int b) {
+    const int begin = cu_q_lens[b], end = cu_q_lens[b + 1], chunk = end - begin;
+    return chunk > 0 && (chunk > max_chunk || begin < 0 || end > num_tokens) ? kNoRoom : chunk;
+  };
   auto bucket = [&](int ctx0, int chunk, int ct) {
     const int t_last = min(chunk, (ct + 1) * tpt) - 1;
     const int n_kv = (ctx0 + t_last) / bn + 1;
     return kPlanBuckets - 1 - min(kPlanBuckets - 1, n_kv >> key_shift);  // heaviest first
   };
   for (int b = tid; b < num_seqs; b += blockDim.x) {
-    const int chunk = cu_q_lens[b + 1] - cu_q_lens[b];
-    const int ctx0 = context_lens[b] - chunk;
+    const int chunk = chunk_of(b);
     if (chunk <= 0) {
       // an empty chunk has a length to check where the weights of its context fade
-      if (tile_starts != nullptr && (context_lens[b] < 0 || context_lens[b] > max_ctx))
+      if (chunk == kNoRoom ||
+          (tile_starts != nullptr && (context_lens[b] < 0 || context_lens[b] > max_ctx)))
         flag_status(status, PA_STATUS_BAD_CONTEXT);
       continue;
     }
+    const int ctx0 = context_lens[b] - chunk;
     if (ctx0 < 0 || context_lens[b] > max_ctx) {  // such a sequence gets no output rows
       flag_status(status, PA_STATUS_BAD_CONTEXT);
       continue;
@@ -211,9 +219,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   __syncthreads();
   for (int b = tid; b < num_seqs; b += blockDim.x) {
-    const int chunk = cu_q_lens[b + 1] - cu_q_lens[b];
+    const int chunk = chunk_of(b);
+    if (chunk <= 0 || context_lens[b] < chunk || context_lens[b] > max_ctx) continue;
     const int ctx0 = context_lens[b] - chunk;
-    if (chunk <= 0 || ctx0 < 0 || context_lens[b] > max_ctx) continue;
     const int ncts = (chunk + tpt - 1) / tpt;
     for (int ct = 0; ct < ncts; ++ct) {
       const int slot = atomicAdd(&s_hist[bucket(ctx0, chunk, ct)], num_kv_heads);
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int each = (num_seqs + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(num_seqs, tid * each), b1 = min(num_seqs, b0 + each);
   auto tiles = [&](int b) {
-    const int chunk = cu_q_lens[b + 1] - cu_q_lens[b], ctx = context_lens[b];
+    const int chunk = chunk_of(b), ctx = context_lens[b];
     return chunk < 0 || ctx < chunk || ctx > max_ctx ? 0 : (ctx + tile_keys - 1) / tile_keys;
   };
   int sum = 0;
@@ -897,14 +905,18 @@ int launch_prefill_t(const PrefillArgs& a, cudaStream_t stream) {
                                             rows_per_item);
   if (items * C::kCtas > 0x7fffffffll)
     return fail(PA_ERR_UNSUPPORTED, "pa_prefill_chunk: grid too large");
+  // the longest chunk that its share of the list has room for
+  const long long max_chunk =
+      items / ((long long)a.num_seqs * a.num_kv_heads) * (rows_per_item / G);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.header = reinterpret_cast<int*>(ws);
   p.items = reinterpret_cast<PrefillItem*>(ws + 256);
   int key_shift = 0;
   while (((long long)a.max_ctx / C::BN + 1) >> key_shift >= kPlanBuckets) ++key_shift;
   cudaError_t e = launch_pdl(prefill_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream,
-                             a.cu_q_lens, a.context_lens, a.num_seqs, a.num_kv_heads, G,
-                             rows_per_item, C::BN, key_shift,
+                             a.cu_q_lens, a.context_lens, a.num_seqs, a.num_tokens, a.num_kv_heads,
+                             G, rows_per_item, (int)std::min<long long>(max_chunk, 0x7fffffffll),
+                             C::BN, key_shift,
                              std::min<long long>(a.max_ctx, (long long)a.max_blocks * a.block_size),
                              reinterpret_cast<PrefillItem*>(ws + 256), reinterpret_cast<int*>(ws),
                              a.status, a.tile_starts, a.tile_keys);
